@@ -12,47 +12,49 @@ namespace {
 
 static_assert(GATED_TILE == HLA2_GATED_SCAN_TILE, "marks are a tile apart");
 
-// The gate a of one token and channel, and z = 1 - a, which for the sigmoid gate is formed by itself and
-// not by subtraction.  fp32 takes the library's exp and an IEEE division.  bf16 takes the hardware's
-// exp2 and reciprocal, each good to one fp32 step (and the argument's rounding, |g| half steps): a
-// bf16 gate's own step is 2^16 times that, and with the exact forms the walk was bound by the vector
-// units (forward over 65536 tokens x 2048 channels, sigmoid: 215 us against 181 us when it was measured).
+// A gate in one register, "held": the factor a, 0 <= a <= 1, as -a where it is small and as z = 1 - a, which is
+// formed by itself and not by subtraction, where it is not.  A gate that holds its state for 1/z tokens is
+// off by z's relative error then, whatever z; 1 - a from a rounded a is off by 2^-25 / z, and every token adds that
+// (9000 tokens of a constant sigmoid gate near logit 12: 4e-3, near 18: 0.5).  The factor not held is 1 minus the
+// one that is, good to half a step.  The sign is the whole sign bit: -0 is a = 0, +0 is z = 0.
+__device__ __forceinline__ bool held_a_itself(float h) { return __builtin_bit_cast(int, h) < 0; }
+__device__ __forceinline__ float held_z(float h) { return held_a_itself(h) ? 1.f + h : h; }
+// a s + y
+__device__ __forceinline__ float scale_add(float h, float s, float y) { return fmaf(-h, s, y) + (held_a_itself(h) ? 0.f : s); }
+// a u
+__device__ __forceinline__ float scale(float h, float u) { return fmaf(-h, u, held_a_itself(h) ? 0.f : u); }
+
+// The gate of one token and channel.  fp32 takes the library's exp and an IEEE division.  bf16 takes the
+// hardware's exp2 and reciprocal, each good to one fp32 step of its result (and the argument's rounding, |g| half
+// steps): with the exact forms the walk was bound by the vector units (forward over 65536 tokens x 2048
+// channels, sigmoid: 215 us against 181 us when it was measured).
 constexpr float LOG2E = 1.44269504088896340736f;
-template <typename T, int GATE> struct Gate {
-  float a, z;
-  __device__ __forceinline__ explicit Gate(float g) {
-    constexpr bool FAST = sizeof(T) == 2;
-    if constexpr (GATE == HLA2_GATE_LOG) {
-      const float m = g > 0.f ? 0.f : g;  // keeps a NaN
-      a = FAST ? __builtin_amdgcn_exp2f(m * LOG2E) : expf(m);
-      z = 1.f;  // the input's factor
-    } else {
-      const float e = FAST ? __builtin_amdgcn_exp2f(-fabsf(g) * LOG2E) : expf(-fabsf(g));
-      const float r = FAST ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
-      a = g < 0.f ? e * r : r;
-      z = g < 0.f ? r : e * r;
-    }
-  }
-};
-template <typename T, int GATE> __device__ __forceinline__ float gate_a(float g) { return Gate<T, GATE>(g).a; }
-// A gate in one register for the backward pass, which uses it three times: log, a, negative where g > 0
-// (a = 1 without a gradient); sigmoid, the smaller of a and z under g's sign, and the larger one is 1
-// minus it, good to half a step since it is at least 1/2.
 template <typename T, int GATE> __device__ __forceinline__ float hold(float g) {
-  const Gate<T, GATE> gate(g);
-  return GATE == HLA2_GATE_LOG ? (g > 0.f ? -1.f : gate.a) : copysignf(g < 0.f ? gate.a : gate.z, g);
+  constexpr bool FAST = sizeof(T) == 2;
+  if constexpr (GATE == HLA2_GATE_LOG) {
+    const float m = g > 0.f ? 0.f : g;  // keeps a NaN
+    return -(FAST ? __builtin_amdgcn_exp2f(m * LOG2E) : expf(m));
+  } else {
+    const float e = FAST ? __builtin_amdgcn_exp2f(-fabsf(g) * LOG2E) : expf(-fabsf(g));
+    const float r = FAST ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
+    return copysignf(e * r, g);  // the smaller of a and z
+  }
 }
-__device__ __forceinline__ bool held_negative(float h) { return __builtin_bit_cast(int, h) < 0; }
-template <int GATE> __device__ __forceinline__ float held_a(float h) {
-  return GATE == HLA2_GATE_LOG ? fabsf(h) : held_negative(h) ? -h : 1.f - h;
+constexpr float HELD_ONE = 0.f;  // a = 1
+// s_t from s_{t-1}: the sigmoid gate moves s towards x by a part z of the way, from the nearer end
+template <int GATE> __device__ __forceinline__ float advance(float h, float x, float s) {
+  return GATE == HLA2_GATE_LOG ? scale_add(h, s, x) : fmaf(-h, s - x, held_a_itself(h) ? x : s);
 }
-template <int GATE> __device__ __forceinline__ float held_z(float h) { return held_negative(h) ? 1.f + h : h; }
-template <int GATE> constexpr float HELD_ONE = GATE == HLA2_GATE_LOG ? 1.f : 0.f;  // a = 1
-// s_t from s_{t-1}: the sigmoid gate mixes, x + a (s - x), so that a state equal to x stays x
-// whatever a's rounding
-template <int GATE> __device__ __forceinline__ float advance(float a, float x, float s) {
-  return GATE == HLA2_GATE_LOG ? fmaf(a, s, x) : fmaf(a, s - x, x);
-}
+
+// The factor of a run of tokens, both ways: A, and Z = 1 - A as the sum of z times the A before it.
+struct Decay {
+  float A = 1.f, Z = 0.f;
+  __device__ __forceinline__ void then(float h) {
+    Z = fmaf(-h, Z, (held_a_itself(h) ? 1.f : Z) + h);
+    A = scale(h, A);
+  }
+  __device__ __forceinline__ float held() const { return A >= 0.5f ? Z : -A; }
+};
 
 __device__ __forceinline__ int seq_len(const int *lens, int b, int n) {
   const int m = lens ? lens[b] : n;
@@ -118,7 +120,7 @@ template <int R, int V> __device__ __forceinline__ void fresh(float (&x)[R][V]) 
 
 // ---------------------------------------------------------------------------
 // Carries between the tiles of one sequence.  A tile is the map s -> A s + H of the state it starts
-// from.  Its workgroup publishes (A, H), then looks back for the newest tile whose outgoing state is
+// from, A held like a gate.  Its workgroup publishes (A, H), then looks back for the newest tile whose outgoing state is
 // known and folds the maps in between onto it, oldest first: the same multiply-adds in the same order
 // as the tiles in between make themselves, so the result does not depend on what was found.
 // What is published is one 64-bit word, written and read whole, so no ordering between words is needed:
@@ -184,7 +186,7 @@ template <int CS> __device__ float look_back(const Word *own, long step, int k) 
     } while (!__all(all));
 #pragma unroll
     for (int m = 0; m < LOOK; ++m)
-      if (i - m >= 1) s = fmaf(map_a(map[m]), s, value(map[m]));
+      if (i - m >= 1) s = scale_add(map_a(map[m]), s, value(map[m]));
   }
   return s;
 }
@@ -226,7 +228,7 @@ template <int CS> __device__ __forceinline__ Word *words_of(const GatedArgs &p, 
   return (Word *)p.words + GATED_WORD0 + ((long)slab * tiles + turn) * 2 * CS + lane;
 }
 
-// Forward.  A thread forms the map of its R tokens, (A, H) with s -> A s + H; the thread rows' maps are
+// Forward.  A thread forms the map of its R tokens, (A, H) with s -> A s + H, A held; the thread rows' maps are
 // folded in LDS in quarters by all threads, the quarters by the first CS, which also carry the state in
 // from the tile before; then every thread walks its tokens again from the state it starts with.
 // Bound by HBM: x and g read once, out written once.  8 x 16 heads x 8192 tokens, d = 128, bf16, log gate:
@@ -237,7 +239,7 @@ template <int CS> __device__ __forceinline__ Word *words_of(const GatedArgs &p, 
 template <typename T, int GATE, bool VEC>
 __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
   using S = Shape<T, VEC>;
-  constexpr bool HOLD = sizeof(T) == 4 || !VEC;  // a takes g's registers; bf16 vectors would need twice as many
+  constexpr bool HOLD = sizeof(T) == 4 || !VEC;  // the gate takes g's registers; bf16 vectors would need twice as many
   constexpr int V = S::V, CG = S::CG, TT = S::TT, R = S::R, CS = S::CS, Q = S::Q, PQ = S::PQ;
   __shared__ float sA[TT][CS], sH[TT][CS], qA[Q][CS], qH[Q][CS], qC[Q][CS];
   const int groups = (p.d + CS - 1) / CS, tiles = (p.n + GATED_TILE - 1) / GATED_TILE;
@@ -264,45 +266,49 @@ __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
     g[r] = ld_pack<T, V>(rg, off);
     x[r] = ld_pack<T, V>(rx, off);
   }
-  float A[V], Hs[V], held[R][V];
+  Decay A[V];
+  float Hs[V], held[R][V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) A[e] = 1.f, Hs[e] = 0.f;
+  for (int e = 0; e < V; ++e) Hs[e] = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float a = t0 + r < len ? gate_a<T, GATE>((float)g[r].e[e]) : 1.f;  // past the end: the state stays
-      if constexpr (HOLD) held[r][e] = a;
-      A[e] *= a;
-      Hs[e] = advance<GATE>(a, (float)x[r].e[e], Hs[e]);
+      const float h = t0 + r < len ? hold<T, GATE>((float)g[r].e[e]) : HELD_ONE;  // past the end: the state stays
+      if constexpr (HOLD) held[r][e] = h;
+      A[e].then(h);
+      Hs[e] = advance<GATE>(h, (float)x[r].e[e], Hs[e]);
     }
 #pragma unroll
-  for (int e = 0; e < V; ++e) sA[tt][cg * V + e] = A[e], sH[tt][cg * V + e] = Hs[e];
+  for (int e = 0; e < V; ++e) sA[tt][cg * V + e] = A[e].held(), sH[tt][cg * V + e] = Hs[e];
   __syncthreads();
   {  // exclusive prefixes of the thread rows within each quarter
     const int c = tid % CS, q = tid / CS;
-    float fA = 1.f, fH = 0.f;
+    Decay fA;
+    float fH = 0.f;
 #pragma unroll
     for (int m = 0; m < PQ; ++m) {
       const float mA = sA[q * PQ + m][c], mH = sH[q * PQ + m][c];
-      sA[q * PQ + m][c] = fA;
+      sA[q * PQ + m][c] = fA.held();
       sH[q * PQ + m][c] = fH;
-      fH = fmaf(mA, fH, mH);
-      fA *= mA;
+      fH = scale_add(mA, fH, mH);
+      fA.then(mA);
     }
-    qA[q][c] = fA;
+    qA[q][c] = fA.held();
     qH[q][c] = fH;
   }
   __syncthreads();
   if (tid < CS) {
     const bool in = c0 + tid < p.d;
     const long o = (long)bh * p.d + c0 + tid;
-    float tA = 1.f, tH = 0.f;
+    Decay run;
+    float tH = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      tH = fmaf(qA[q][tid], tH, qH[q][tid]);
-      tA *= qA[q][tid];
+      tH = scale_add(qA[q][tid], tH, qH[q][tid]);
+      run.then(qA[q][tid]);
     }
+    const float tA = run.held();
     float s;
     if (k == 0) {
       s = p.s0 && in ? p.s0[o] : 0.f;
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
       publish_map(w, tA, tH);
       s = look_back<CS>(w, 2 * CS, k);
     }
-    const float last = fmaf(tA, s, tH);
+    const float last = scale_add(tA, s, tH);
     if (k + 1 < used) publish_state(words_of<CS>(p, at.slab, k, tiles, tid) + CS, last);
     if (in) {
       if (p.marks_out) p.marks_out[((long)bh * tiles + k) * p.d + c0 + tid] = s;
@@ -320,22 +326,23 @@ __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       qC[q][tid] = s;
-      s = fmaf(qA[q][tid], s, qH[q][tid]);
+      s = scale_add(qA[q][tid], s, qH[q][tid]);
     }
   }
   __syncthreads();
   fresh(x);
-  if constexpr (!HOLD) fresh(g);
+  if constexpr (HOLD) fresh(held);
+  else fresh(g);
   float s[V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = fmaf(sA[tt][cg * V + e], qC[tt / PQ][cg * V + e], sH[tt][cg * V + e]);
+  for (int e = 0; e < V; ++e) s[e] = scale_add(sA[tt][cg * V + e], qC[tt / PQ][cg * V + e], sH[tt][cg * V + e]);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     Pack<V, T> y;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float a = HOLD ? held[r][e] : gate_a<T, GATE>((float)g[r].e[e]);
-      s[e] = advance<GATE>(a, (float)x[r].e[e], s[e]);  // rows past the end are dropped
+      const float h = HOLD ? held[r][e] : hold<T, GATE>((float)g[r].e[e]);
+      s[e] = advance<GATE>(h, (float)x[r].e[e], s[e]);  // rows past the end are dropped
       y.e[e] = (T)s[e];
     }
     st_pack<T, V>(ro, ch < p.d && t0 + r < len ? (t0 + r) * row + ch * (int)sizeof(T) : OOB_OFFSET, y);
@@ -371,6 +378,7 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
                                rdx = buf_rsrc((const T *)p.dx + base, bytes), rdg = buf_rsrc((const T *)p.dg + base, bytes);
   Pack<V, T> x[R], y[R];
   float h[R][V];  // the gates
+  constexpr float NO_GRADIENT = HELD_ONE;  // of log gates, a = 1 that does not depend on g
   {
     Pack<V, T> g[R];
 #pragma unroll
@@ -383,49 +391,57 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[r][e] = t0 + r < len ? hold<T, GATE>((float)g[r].e[e]) : HELD_ONE<GATE>;  // past the end: the states stay
+      for (int e = 0; e < V; ++e) {
+        const float gv = (float)g[r].e[e];
+        h[r][e] = t0 + r < len ? hold<T, GATE>(gv) : HELD_ONE;  // past the end: the states stay
+        if (GATE == HLA2_GATE_LOG && gv > 0.f) h[r][e] = NO_GRADIENT;
+      }
   }
   {
-    float A[V], Hs[V], U[V];
+    Decay A[V];
+    float Hs[V], U[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) A[e] = 1.f, Hs[e] = 0.f, U[e] = 0.f;
+    for (int e = 0; e < V; ++e) Hs[e] = 0.f, U[e] = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float a = held_a<GATE>(h[r][e]);
-        A[e] *= a;
-        Hs[e] = advance<GATE>(a, (float)x[r].e[e], Hs[e]);
+        A[e].then(h[r][e]);
+        Hs[e] = advance<GATE>(h[r][e], (float)x[r].e[e], Hs[e]);
       }
+    }
+    fresh(h);
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r) U[e] = held_a<GATE>(h[r][e]) * ((float)y[r].e[e] + U[e]);
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r) U[e] = scale(h[r][e], (float)y[r].e[e] + U[e]);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) sA[tt][cg * V + e] = A[e], sH[tt][cg * V + e] = Hs[e], sU[tt][cg * V + e] = U[e];
+    for (int e = 0; e < V; ++e) sA[tt][cg * V + e] = A[e].held(), sH[tt][cg * V + e] = Hs[e], sU[tt][cg * V + e] = U[e];
   }
   __syncthreads();
   {
     const int c = tid % CS, q = tid / CS;
-    float mA[PQ], fA = 1.f, fH = 0.f;
+    Decay fA, bA;
+    float mA[PQ], fH = 0.f, bU = 0.f;
 #pragma unroll
     for (int m = 0; m < PQ; ++m) {
       mA[m] = sA[q * PQ + m][c];
       const float mH = sH[q * PQ + m][c];
-      sA[q * PQ + m][c] = fA;
+      sA[q * PQ + m][c] = fA.held();
       sH[q * PQ + m][c] = fH;
-      fH = fmaf(mA[m], fH, mH);
-      fA *= mA[m];
+      fH = scale_add(mA[m], fH, mH);
+      fA.then(mA[m]);
     }
-    qA[q][c] = fA;
+    qA[q][c] = fA.held();
     qH[q][c] = fH;
-    float bA = 1.f, bU = 0.f;
 #pragma unroll
     for (int m = PQ - 1; m >= 0; --m) {
       const float mU = sU[q * PQ + m][c];
-      sB[q * PQ + m][c] = bA;
+      sB[q * PQ + m][c] = bA.held();
       sU[q * PQ + m][c] = bU;
-      bU = fmaf(mA[m], bU, mU);
-      bA *= mA[m];
+      bU = scale_add(mA[m], bU, mU);
+      bA.then(mA[m]);
     }
     qU[q][c] = bU;
   }
@@ -438,14 +454,16 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       qC[q][tid] = s;
-      s = fmaf(qA[q][tid], s, qH[q][tid]);
+      s = scale_add(qA[q][tid], s, qH[q][tid]);
     }
-    float tA = 1.f, tU = 0.f;
+    Decay run;
+    float tU = 0.f;
 #pragma unroll
     for (int q = Q - 1; q >= 0; --q) {
-      tU = fmaf(qA[q][tid], tU, qU[q][tid]);
-      tA *= qA[q][tid];
+      tU = scale_add(qA[q][tid], tU, qU[q][tid]);
+      run.then(qA[q][tid]);
     }
+    const float tA = run.held();
     float u;
     if (turn == 0) {
       u = p.ds_last && in ? p.ds_last[o] : 0.f;
@@ -454,13 +472,13 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
       publish_map(w, tA, tU);
       u = look_back<CS>(w, 2 * CS, turn);
     }
-    const float first = fmaf(tA, u, tU);
+    const float first = scale_add(tA, u, tU);
     if (k > 0) publish_state(words_of<CS>(p, at.slab, turn, tiles, tid) + CS, first);
     if (in && p.ds0 && k == 0) p.ds0[o] = first;
 #pragma unroll
     for (int q = Q - 1; q >= 0; --q) {
       qD[q][tid] = u;
-      u = fmaf(qA[q][tid], u, qU[q][tid]);
+      u = scale_add(qA[q][tid], u, qU[q][tid]);
     }
   }
   __syncthreads();
@@ -471,8 +489,8 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const int c = cg * V + e, q = tt / PQ;
-    s[e] = fmaf(sA[tt][c], qC[q][c], sH[tt][c]);
-    u[e] = fmaf(sB[tt][c], qD[q][c], sU[tt][c]);
+    s[e] = scale_add(sA[tt][c], qC[q][c], sH[tt][c]);
+    u[e] = scale_add(sB[tt][c], qD[q][c], sU[tt][c]);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -480,7 +498,7 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
     for (int e = 0; e < V; ++e) {
       const float xv = (float)x[r].e[e];
       before[r][e] = GATE == HLA2_GATE_LOG ? s[e] : s[e] - xv;
-      s[e] = advance<GATE>(held_a<GATE>(h[r][e]), xv, s[e]);
+      s[e] = advance<GATE>(h[r][e], xv, s[e]);
     }
   fresh(h);
 #pragma unroll
@@ -489,12 +507,12 @@ __global__ void __launch_bounds__(256, 2) gated_backward_kernel(GatedArgs p) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float d = (float)y[r].e[e] + u[e];
-      u[e] = held_a<GATE>(h[r][e]) * d;
+      u[e] = scale(h[r][e], d);
       if constexpr (GATE == HLA2_GATE_LOG) {
         ox.e[e] = (T)d;
-        og.e[e] = (T)(h[r][e] < 0.f ? 0.f : u[e] * before[r][e]);
+        og.e[e] = (T)(__builtin_bit_cast(int, h[r][e]) == 0 ? 0.f : u[e] * before[r][e]);
       } else {
-        const float z = held_z<GATE>(h[r][e]);
+        const float z = held_z(h[r][e]);
         ox.e[e] = (T)(z * d);
         og.e[e] = (T)(u[e] * z * before[r][e]);
       }
@@ -514,7 +532,7 @@ template <typename T, int GATE>
 __global__ void __launch_bounds__(256) gated_step_kernel(GatedStepArgs p) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long)p.N * p.Hd || (p.pos && p.pos[i / p.Hd] < 0)) return;
-  const float s = advance<GATE>(gate_a<T, GATE>((float)((const T *)p.g)[i]), (float)((const T *)p.x)[i], p.state[i]);
+  const float s = advance<GATE>(hold<T, GATE>((float)((const T *)p.g)[i]), (float)((const T *)p.x)[i], p.state[i]);
   p.state[i] = s;
   ((T *)p.out)[i] = (T)s;
 }

@@ -16,6 +16,7 @@ import torch
 
 from causal_prefix_scan_hla2_amd import hla2 as H
 from oracle import mixers as M
+from tests.parity import TOL_BF16, TOL_F32, rel_l2
 
 pytestmark = pytest.mark.gpu
 
@@ -307,3 +308,68 @@ def test_nan_gate_of_any_payload(dtype, gate):
     out, dx = torch.isnan(got["out"][0, 0]), torch.isnan(got["dx"][0, 0])
     assert out[300:, 5].all() and out.sum() == 800
     assert dx[:300, 5].all() and not dx[301:].any() and not dx[:, torch.arange(64, device=dx.device) != 5].any()
+
+
+# Gates that hold: 1 - a far below a's own rounding step.  What counts there is the relative error of 1 - a, so
+# the results meet the bars of tests/parity.py in the 2-norm: 1e-4 for all results of fp32 inputs and for the fp32
+# states of bf16 ones, 2e-2 for bf16 outputs.  (A token rounds the state by at most u; over the 9000 tokens here
+# that adds up to sqrt(9000) u = 6e-6 in the root mean square, and to a few times that with the tiles' own.)
+def gates_that_hold(gate, mean, constant, n, seed, dtype):
+    c = draw(1, 2, n, 24, dtype, gate, seed=seed)
+    gen = torch.Generator().manual_seed(seed + 1)
+    r = torch.randn(1, 2, 1 if constant else n, 24, generator=gen)
+    g = mean + r if gate == M.SIGMOID else -mean * torch.exp(r)
+    c["g"] = g.expand(1, 2, n, 24).to(DT[dtype]).contiguous()
+    return c
+
+
+def norms(c, gate, use_s0, dtype):
+    got = call(c, gate, use_s0=use_s0)
+    x, g, dout = f64(c["x"]), f64(c["g"]), f64(c["dout"])
+    s0, dl = (f64(c["s0"]), f64(c["ds_last"])) if use_s0 else (None, None)
+    s, last = M.gated_scan(x, g, gate, s0)
+    dx, dg, ds0 = M.gated_scan_backward(x, g, gate, dout, s0, dl)
+    err = {}
+    for k, ref in dict(out=s, last=last, dx=dx, dg=dg, ds0=ds0).items():
+        err[k] = rel_l2(f64(got[k]), ref)
+    print(gate, err)
+    assert all(e <= (TOL_F32 if dtype == "f32" or k in ("last", "ds0") else TOL_BF16) for k, e in err.items()), err
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("use_s0", [False, True])
+@pytest.mark.parametrize("constant", [False, True])
+@pytest.mark.parametrize("mean", [8, 10, 12, 14, 16, 18])
+def test_sigmoid_gates_that_hold(mean, constant, use_s0, dtype):
+    norms(gates_that_hold(M.SIGMOID, mean, constant, 9000, 70 + mean, dtype), M.SIGMOID, use_s0, dtype)
+
+
+def test_one_token_of_a_sigmoid_gate_that_holds():
+    """s = (1 - a) x from a zero state: 1 - a to a few roundings (exp with its argument rounded by |g| u, the sum, the
+    division, two products: (8 + |g|) u), in the forward call and in the step."""
+    g = torch.tensor([3.0, 9.0, 14.0, 17.0, 20.0, 40.0, 80.0])
+    want = 1 / (1 + np.exp(f64(g)))
+    dev = torch.device("cuda:0")
+    for dtype in ("f32", "bf16"):
+        gd = g.to(DT[dtype]).to(dev).view(1, 7)  # every value is one of bf16
+        x, st, out = torch.ones_like(gd), torch.zeros(1, 7, device=dev), torch.empty_like(gd)
+        H.hla2_gated_scan_step(st, x, gd, out, gate=M.SIGMOID)
+        last, o = torch.empty(1, 7, device=dev), torch.empty(1, 1, 7, dtype=DT[dtype], device=dev)
+        H.hla2_gated_scan_forward(x.view(1, 1, 7), gd.view(1, 1, 7), o, gate=M.SIGMOID, s_last=last)
+        for s in (st, last):
+            assert (np.abs(f64(s)[0] - want) <= (8 + f64(g)) * U * want).all()
+
+
+def test_an_open_sigmoid_gate_holds_its_state():
+    """a = 1 to fp32 and 1 - a = 0: the state keeps its bits, whatever the inputs."""
+    dev = torch.device("cuda:0")
+    for dtype in ("f32", "bf16"):
+        c = draw(1, 1, 1500, 40, dtype, M.SIGMOID, seed=77)
+        c["g"].fill_(200.0)
+        c["x"].mul_(1000.0)
+        got = call(c, M.SIGMOID)
+        assert torch.equal(got["last"].cpu(), c["s0"])
+        assert torch.equal(got["out"].cpu(), c["s0"][:, :, None].to(DT[dtype]).expand_as(c["x"]))
+        st, o = c["s0"].to(dev).clone(), torch.empty(1, 1, 40, dtype=DT[dtype], device=dev)
+        H.hla2_gated_scan_step(st, c["x"][:, :, 0].contiguous().to(dev), c["g"][:, :, 0].contiguous().to(dev), o, gate=M.SIGMOID)
+        assert torch.equal(st.cpu(), c["s0"])
