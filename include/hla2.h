@@ -314,9 +314,9 @@ int hla2_ho3_forward(const void *q, const void *k, const void *v, void *out,
  * A log gate of -inf gives a_t = 0: the token starts a new sequence.  Log gates
  * above 0 count as 0.  States are fp32; out is rounded once to `dtype`.  The
  * sigmoid gate is applied as x + a (s - x), or from z = 1 - a, formed by itself, as
- * s + z (x - s) where a is the larger of the two, so gates that hold a state for
- * long are as exact as others.  NaN and Inf stay in their channel and after their
- * token; an Inf may become NaN (by these differences).
+ * s + z (x - s) where a is the larger of the two, a log gate near 0 as s + (x - z s),
+ * so gates that hold a state for long are as exact as others.  NaN and Inf stay in
+ * their channel and after their token; an Inf may become NaN (by these differences).
  *   x, g : [B, H, n, d]   element type `dtype` (any d >= 1; [B, n, C] is H = 1)
  *   out  : [B, H, n, d]   element type `dtype` (written)
  *   s0     : nullable [B, H, d] fp32, the state before the first token (NULL: zero)

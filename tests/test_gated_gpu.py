@@ -373,3 +373,31 @@ def test_an_open_sigmoid_gate_holds_its_state():
         st, o = c["s0"].to(dev).clone(), torch.empty(1, 1, 40, dtype=DT[dtype], device=dev)
         H.hla2_gated_scan_step(st, c["x"][:, :, 0].contiguous().to(dev), c["g"][:, :, 0].contiguous().to(dev), o, gate=M.SIGMOID)
         assert torch.equal(st.cpu(), c["s0"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("use_s0", [False, True])
+@pytest.mark.parametrize("constant", [False, True])
+@pytest.mark.parametrize("size", [1e-2, 1e-3, 1e-4, 1e-5, 1e-6])
+def test_log_gates_that_hold(size, constant, use_s0, dtype):
+    """Constant decays over 40000 tokens: sqrt(40000) u = 1.2e-5 in the root mean square."""
+    norms(gates_that_hold(M.LOG, size, constant, 40000, 90, dtype), M.LOG, use_s0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decay_of_a_state_by_a_log_gate(dtype):
+    """n tokens of one gate and no input: s = exp(n g) s0.  A token's factor is off by at most 4 u of 1 - a (the series' rest, three multiply-adds and
+    one product) or 4 u of a, and its product by u / 2; so 4 u n |g| + u n in all, and 12 u for the tiles' maps
+    of each 256 tokens."""
+    n, g = 5000, torch.tensor([-2.0 ** -k for k in range(2, 24)])
+    c = dict(x=torch.zeros(1, 1, n, 22), g=g.expand(1, 1, n, 22).contiguous(), s0=torch.ones(1, 1, 22),
+             dout=torch.zeros(1, 1, n, 22), ds_last=torch.ones(1, 1, 22))
+    for k in ("x", "g", "dout"):
+        c[k] = c[k].to(DT[dtype])
+    got = call(c, M.LOG)
+    t = np.arange(1, n + 1)[:, None]
+    want = np.exp(t * f64(g)[None])
+    err = U * (4 * t * np.abs(f64(g)) + t + 12 * (t // 256 + 1)) * want
+    near(f64(got["out"])[0, 0], want, err, dtype, "out")
+    for k in ("last", "ds0"):
+        near(f64(got[k])[0, 0], want[-1], err[-1], "f32", k)
