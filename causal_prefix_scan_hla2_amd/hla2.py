@@ -351,6 +351,8 @@ def _launch(name, check, t, stream, *args):
     here = t.get_device()
     if here < 0:
         raise ValueError("tensors must be on the GPU")
+    if stream is not None and getattr(stream, "device_index", here) != here:
+        raise ValueError("stream must be one of the tensors' device")
     fn = getattr(_lib or lib(), name)
     # the raw handle, 0.2 us; building a Stream object for it takes 5 us, half of a small call
     s = torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
@@ -401,16 +403,24 @@ def _int(x, name):
     return x
 
 
-def _workspace(workspace, need, like, stream):
-    """(workspace tensor or None, its bytes); allocated here when the caller gives none, and then held
-    by the allocator until the given stream has passed the call."""
+def _scratch(need, like, stream):
+    """`need` bytes on like's device from the memory of the stream that the call runs on: what the allocator hands
+    out there, and takes back when the call returns, is ordered with that stream's work alone.  (A block of the
+    current stream's memory may still be in use by work that the given stream does not wait for.)"""
     import torch
+    if stream is None or not like.is_cuda:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
+def _workspace(workspace, need, like, stream):
+    """(workspace tensor or None, its bytes); allocated here when the caller gives none."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        if stream is not None and workspace.is_cuda:
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
+        workspace = _scratch(need, like, stream)
     elif not workspace.is_contiguous() or workspace.device != like.device:
         raise ValueError("workspace must be contiguous and on %s" % like.device)
     return workspace, workspace.numel() * workspace.element_size()
