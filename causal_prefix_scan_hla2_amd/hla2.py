@@ -179,7 +179,6 @@ def hla2_forward(q, k, v, out, decay=1.0, normalize=False, chunk=64, den_out=Non
     uint8 device tensor of at least the required bytes; allocated here (torch
     caching allocator) when None.  Returns the C return code (and raises on
     error when check=True)."""
-    import torch
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -187,7 +186,7 @@ def hla2_forward(q, k, v, out, decay=1.0, normalize=False, chunk=64, den_out=Non
             raise ValueError("tensors must be contiguous")
     need = hla2_forward_workspace_bytes(B, H, n, d, dv, chunk, segments)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, H, n, d, dv, float(decay), int(bool(normalize)), int(chunk),
             _dtype_code(q), _ptr(den_out), _ptr(workspace), wbytes)
@@ -240,7 +239,7 @@ def hla2_forward_state(q, k, v, out, state_out, decay=1.0, normalize=False, chun
         raise ValueError("state_out must be fp32 [B, H, state_floats]")
     need = hla2_forward_state_workspace_bytes(B, H, n, d, dv, chunk, segments)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().hla2_forward_state(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, H, n, d, dv, float(decay),
                                   int(bool(normalize)), int(chunk), _dtype_code(q), _ptr(den_out),
@@ -259,7 +258,6 @@ def hla2_backward(q, k, v, dout, grad_q, grad_k, grad_v, decay=1.0, normalize=Fa
     """Call ``hla2_backward``: gradients of sum(dout * out) w.r.t. q, k, v written to
     grad_q, grad_k: [B,H,n,d] and grad_v: [B,H,n,dv] (same dtype as q).  Under
     ``normalize`` the forward's ``out`` and fp32 ``den`` are required."""
-    import torch
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, dout, grad_q, grad_k, grad_v) + ((out, den) if normalize else ()):
@@ -268,7 +266,7 @@ def hla2_backward(q, k, v, dout, grad_q, grad_k, grad_v, decay=1.0, normalize=Fa
     code = _dtype_code(q)
     need = hla2_backward_workspace_bytes(B, H, n, d, dv, normalize, code, segments)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().hla2_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out) if normalize else None,
                              _ptr(den) if normalize else None, _ptr(dout), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v),
@@ -287,7 +285,6 @@ def hla2_ahla_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, wo
                       segments=0, check=True) -> int:
     """Call ``hla2_ahla_forward`` (the asymmetric variant) on torch tensors q, k: [B,H,n,d];
     v, out: [B,H,n,dv]."""
-    import torch
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -296,7 +293,7 @@ def hla2_ahla_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, wo
     code = _dtype_code(q)
     need = hla2_ahla_forward_workspace_bytes(B, H, n, d, dv, code, segments)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().hla2_ahla_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, H, n, d, dv, float(decay),
                                  int(bool(normalize)), code, _ptr(den_out), _ptr(workspace), wbytes, int(segments),
@@ -313,7 +310,6 @@ def hla2_ho3_forward_workspace_bytes(B, H, n, d, dv, dtype_code, segments=0) -> 
 def hla2_ho3_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, workspace=None, stream=None,
                      segments=0, check=True) -> int:
     """Call ``hla2_ho3_forward`` (third order) on torch tensors q, k: [B,H,n,d]; v, out: [B,H,n,dv]."""
-    import torch
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -322,7 +318,7 @@ def hla2_ho3_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, wor
     code = _dtype_code(q)
     need = hla2_ho3_forward_workspace_bytes(B, H, n, d, dv, code, segments)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = lib().hla2_ho3_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), B, H, n, d, dv, float(decay),
                                 int(bool(normalize)), code, _ptr(den_out), _ptr(workspace), wbytes, int(segments),

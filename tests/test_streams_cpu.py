@@ -48,3 +48,29 @@ def test_no_workspace_is_taken_where_none_is_needed(taken):
 def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="stream"):
         H._launch("hla2_gated_scan_step", True, LIKE, types.SimpleNamespace(cuda_stream=4096, device_index=1))
+
+
+class Stub:
+    """A library whose every call succeeds and whose every workspace is 64 bytes (or floats)."""
+
+    def __getattr__(self, name):
+        return lambda *args: 64 if name.endswith("_bytes") or name.endswith("_floats") else 0
+
+
+X = torch.zeros(1, 1, 4, 8)
+CALLS = {
+    "forward": lambda s: H.hla2_forward(X, X, X, X, stream=s),
+    "state": lambda s: H.hla2_forward_state(X, X, X, X, torch.zeros(64), stream=s),
+    "backward": lambda s: H.hla2_backward(X, X, X, X, X, X, X, stream=s),
+    "ahla": lambda s: H.hla2_ahla_forward(X, X, X, X, stream=s),
+    "ho3": lambda s: H.hla2_ho3_forward(X, X, X, X, stream=s),
+}
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_every_call_takes_its_workspace_so(call, monkeypatch):
+    seen = []
+    monkeypatch.setattr(H, "lib", Stub)
+    monkeypatch.setattr(H, "_scratch", lambda need, like, stream: seen.append((need, stream)) or torch.zeros(need, dtype=torch.uint8))
+    assert CALLS[call](STREAM) == 0
+    assert seen == [(64, STREAM)]

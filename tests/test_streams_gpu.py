@@ -50,6 +50,22 @@ def step(seed):
     return lambda stream: H.hla2_window_step(ck, cv, pos, q, k, v, out, window, stream=stream), (out, ck, cv)
 
 
+def linear(seed):
+    """The linear forms' entry points."""
+    gen = torch.Generator(DEV).manual_seed(seed)
+    q, k, v, dout = (randn(gen, 2, 8, 4096, 64) / 8 for _ in range(4))
+    outs = [torch.zeros_like(q) for _ in range(7)]
+    state = torch.zeros(2, 8, H.hla2_state_floats(64, 64), device=DEV)
+
+    def run(stream):
+        H.hla2_forward(q, k, v, outs[0], decay=0.98, stream=stream)
+        H.hla2_forward_state(q, k, v, outs[1], state, decay=0.98, stream=stream)
+        H.hla2_backward(q, k, v, dout, outs[2], outs[3], outs[4], decay=0.98, stream=stream)
+        H.hla2_ahla_forward(q, k, v, outs[5], decay=0.98, stream=stream)
+        H.hla2_ho3_forward(q, k, v, outs[6], decay=0.98, stream=stream)
+    return run, (*outs, state)
+
+
 def check(make, other):
     first, second, alone = make(1), make(2), make(2)
     alone[0](None)
@@ -67,7 +83,7 @@ def check(make, other):
         assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("make", [scan, window, step])
+@pytest.mark.parametrize("make", [scan, window, step, linear])
 @pytest.mark.parametrize("handle", ["stream", "int"])
 def test_back_to_back_on_two_streams(make, handle):
     s = torch.cuda.Stream(DEV)
@@ -76,7 +92,7 @@ def test_back_to_back_on_two_streams(make, handle):
 
 def test_the_default_stream_by_its_handle():
     """0 is a stream like others: the calls' results are those without a stream."""
-    for make in (scan, window, step):
+    for make in (scan, window, step, linear):
         (run, got), (alone, want) = make(3), make(3)
         alone(None)
         run(0)
