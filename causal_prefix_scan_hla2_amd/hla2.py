@@ -179,6 +179,7 @@ def hla2_forward(q, k, v, out, decay=1.0, normalize=False, chunk=64, den_out=Non
     uint8 device tensor of at least the required bytes; allocated here (torch
     caching allocator) when None.  Returns the C return code (and raises on
     error when check=True)."""
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -208,6 +209,7 @@ def hla2_forward_noalloc(q, k, v, out, decay=1.0, normalize=False, chunk=64, den
                          check=True) -> int:
     """Call the C forward pass that uses the library's fixed device workspace (no allocation here
     or in the library).  Same tensors and results as hla2_forward."""
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -230,6 +232,7 @@ def hla2_forward_state(q, k, v, out, state_out, decay=1.0, normalize=False, chun
     final state, written to ``state_out`` (fp32 [B,H,state_floats], the layout
     ``hla2_decode_step`` reads).  ``workspace`` as for ``hla2_forward``."""
     import torch
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out, state_out):
@@ -258,6 +261,7 @@ def hla2_backward(q, k, v, dout, grad_q, grad_k, grad_v, decay=1.0, normalize=Fa
     """Call ``hla2_backward``: gradients of sum(dout * out) w.r.t. q, k, v written to
     grad_q, grad_k: [B,H,n,d] and grad_v: [B,H,n,dv] (same dtype as q).  Under
     ``normalize`` the forward's ``out`` and fp32 ``den`` are required."""
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, dout, grad_q, grad_k, grad_v) + ((out, den) if normalize else ()):
@@ -285,6 +289,7 @@ def hla2_ahla_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, wo
                       segments=0, check=True) -> int:
     """Call ``hla2_ahla_forward`` (the asymmetric variant) on torch tensors q, k: [B,H,n,d];
     v, out: [B,H,n,dv]."""
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -310,6 +315,7 @@ def hla2_ho3_forward_workspace_bytes(B, H, n, d, dv, dtype_code, segments=0) -> 
 def hla2_ho3_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, workspace=None, stream=None,
                      segments=0, check=True) -> int:
     """Call ``hla2_ho3_forward`` (third order) on torch tensors q, k: [B,H,n,d]; v, out: [B,H,n,dv]."""
+    _sizes(q, v)
     B, H, n, d = q.shape
     dv = v.shape[-1]
     for t in (q, k, v, out):
@@ -331,6 +337,7 @@ def hla2_ho3_forward(q, k, v, out, decay=1.0, normalize=False, den_out=None, wor
 def hla2_decode_step(state, q, k, v, out, decay=1.0, normalize=False, stream=None, check=True) -> int:
     """Call ``hla2_decode_step``: state [N,H,state_floats] fp32 (in place);
     q, k: [N,H,d]; v, out: [N,H,dv]."""
+    _sizes(q, v)
     N, H, d = q.shape
     dv = v.shape[-1]
     rc = lib().hla2_decode_step(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(out), N, H, d, dv, float(decay),
@@ -399,6 +406,14 @@ def _int(x, name):
     return x
 
 
+def _sizes(*tensors):
+    """The same for the sizes of tensors, which the calls take from their shapes."""
+    for t in tensors:
+        if t.numel() > 2147483647:  # else every size fits, or one is 0 and refused as that
+            for size in t.shape:
+                _int(size, "every size")
+
+
 def _scratch(need, like, stream):
     """`need` bytes on like's device from the memory of the stream that the call runs on: what the allocator hands
     out there, and takes back when the call returns, is ordered with that stream's work alone.  (A block of the
@@ -424,13 +439,15 @@ def _workspace(workspace, need, like, stream):
 
 @functools.lru_cache(maxsize=256)
 def hla2_gated_scan_workspace_bytes(B, H, n, d, dtype_code) -> int:
-    return int(lib().hla2_gated_scan_workspace_bytes(B, H, n, d, int(dtype_code)))
+    sizes = (_int(x, "every size") for x in (B, H, n, d))
+    return int(lib().hla2_gated_scan_workspace_bytes(*sizes, int(dtype_code)))
 
 
 def _gated_shapes(x):
     import torch
     if x.dim() not in (3, 4):
         raise ValueError("x must be [B, H, n, d] or [B, n, d]")
+    _sizes(x)
     B, n, d = x.shape[0], x.shape[-2], x.shape[-1]
     H = x.shape[1] if x.dim() == 4 else 1
     tiles = (n + HLA2_GATED_SCAN_TILE - 1) // HLA2_GATED_SCAN_TILE
@@ -487,6 +504,7 @@ def hla2_gated_scan_step(state, x, g, out, gate=HLA2_GATE_LOG, pos=None, stream=
         (N, d), H = shape, 1
     else:
         raise ValueError("x must be [N, H, d] or [N, d]")
+    _sizes(x)
     code = _dtype_code(x)
     _expect_all(x.dtype, here, ((x, "x", shape), (g, "g", shape), (out, "out", shape)))
     _expect(state, "state", shape, torch.float32, here)
@@ -503,6 +521,7 @@ def _window_shapes(q, k, v):
         raise ValueError("q, k, v must be [B, H, n, d], [B, Hkv, n, d], [B, Hkv, n, dv]")
     B, H, n, d = qs
     Hkv, dv = ks[1], vs[3]
+    _sizes(q, k, v)
     _expect_all(q.dtype, q.get_device(), ((q, "q", qs), (k, "k", (B, Hkv, n, d)), (v, "v", (B, Hkv, n, dv))))
     return B, H, Hkv, n, d, dv
 
@@ -526,7 +545,8 @@ def hla2_window_forward(q, k, v, out, window, sinks=0, scale=None, lse=None, len
 
 @functools.lru_cache(maxsize=256)
 def hla2_window_backward_workspace_bytes(B, H, Hkv, n, d, dv, window, sinks, dtype_code) -> int:
-    return int(lib().hla2_window_backward_workspace_bytes(B, H, Hkv, n, d, dv, window, sinks, int(dtype_code)))
+    sizes = (_int(x, "every size") for x in (B, H, Hkv, n, d, dv, window, sinks))
+    return int(lib().hla2_window_backward_workspace_bytes(*sizes, int(dtype_code)))
 
 
 def hla2_window_backward(q, k, v, out, lse, dout, dq, dk, dv, window, sinks=0, scale=None, lens=None, workspace=None,
@@ -565,7 +585,8 @@ def hla2_window_cache(k, v, cache_k, cache_v, window, sinks=0, lens=None, stream
 
 @functools.lru_cache(maxsize=256)
 def hla2_window_step_workspace_bytes(N, H, Hkv, d, dv, window, sinks, dtype_code) -> int:
-    return int(lib().hla2_window_step_workspace_bytes(N, H, Hkv, d, dv, window, sinks, int(dtype_code)))
+    sizes = (_int(x, "every size") for x in (N, H, Hkv, d, dv, window, sinks))
+    return int(lib().hla2_window_step_workspace_bytes(*sizes, int(dtype_code)))
 
 
 def hla2_window_step(cache_k, cache_v, pos, q, k, v, out, window, sinks=0, scale=None, workspace=None, stream=None,
@@ -579,6 +600,7 @@ def hla2_window_step(cache_k, cache_v, pos, q, k, v, out, window, sinks=0, scale
         raise ValueError("q, k, v must be [N, H, d], [N, Hkv, d], [N, Hkv, dv]")
     N, H, d = qs
     Hkv, dv, slots = ks[1], vs[2], window + sinks
+    _sizes(q, k, v)
     here = q.get_device()
     _expect_all(q.dtype, here, ((q, "q", qs), (k, "k", (N, Hkv, d)), (v, "v", (N, Hkv, dv)),
                                 (out, "out", (N, H, dv)), (cache_k, "cache_k", (N, Hkv, slots, d)),
