@@ -28,10 +28,8 @@ int check_shape(int B, int H, int Hkv, int n, int d, int dv, int window, int sin
   if ((long)n > (1L << 30) || (long)B * H * n > (1L << 40)) return HLA2_ERR_UNSUPPORTED;
   // one head's rows are addressed with 32-bit byte offsets
   if ((long)n * ((d > dv ? d : dv) + 16) * 4 > 0x7fffff00L) return HLA2_ERR_UNSUPPORTED;
-  // launches of 256 threads to 64 rows of a head (16 rows in the backward's row products) stay below
-  // 2^32 work-items
-  if (((long)B * H * (((long)n + 63) / 64) + 8) * 256 > 0xFFFFFFFFL || ((long)B * H * n + 15) / 16 * 256 > 0xFFFFFFFFL)
-    return HLA2_ERR_UNSUPPORTED;
+  // launches of 256 threads to 64 rows of a head stay below 2^32 work-items
+  if (((long)B * H * (((long)n + 63) / 64) + 8) * 256 > 0xFFFFFFFFL) return HLA2_ERR_UNSUPPORTED;
   return HLA2_OK;
 }
 

@@ -399,8 +399,9 @@ int hla2_gated_scan_step(float *state, const void *x, const void *g, void *out, 
  *   window >= 1 (window >= n: causal attention), 0 <= sinks <= HLA2_WINDOW_MAX_SINKS,
  *   scale > 0 and finite (below 2^126)
  * Outputs overlap neither the inputs nor each other, here and in the calls below.
- * Supported: d, dv multiples of 16 up to 128 (fp32: up to 64); the other limits and
- * errors as for hla2_forward; tensors 16-byte aligned.  For finite inputs a row
+ * Supported: d, dv multiples of 16 up to 128 (fp32: up to 64); B * H * ceil(n / 64)
+ * below 2^24 - 8; the other limits and errors as for hla2_forward; tensors 16-byte
+ * aligned.  For finite inputs a row
  * does not depend on tokens it does not see; a NaN or Inf in a token before the
  * sequence's end can reach rows that do not see it (0 * Inf = NaN).
  */

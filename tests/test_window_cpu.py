@@ -149,3 +149,23 @@ def test_backward_launch_limit(L):
     assert H.hla2_window_backward_workspace_bytes(*ints(kw, *ALL), 1) == 0
     assert H.hla2_window_backward_workspace_bytes(*ints(dict(kw, window=20), *ALL), 1) > 0  # no far queries
     assert L.hla2_window_backward(P, P, P, P, P, P, P, P, P, None, *ints(kw, *ALL), 1.0, 1, P, 1 << 40, None) == UNS
+
+
+def test_launch_limits_are_those_of_64_rows(L):
+    """B H ceil(n / 64) below 2^24 - 8, whatever B H n: the shape passes where the next check, of alignment, is what
+    refuses the call."""
+    def code(call, **kw):
+        if call == "cache":
+            return L.hla2_window_cache(ODD, P, P, P, None, *ints(kw, "B", "Hkv", "n", "d", "dv", "window", "sinks"), 1, None)
+        if call == "forward":
+            return L.hla2_window_forward(ODD, P, P, P, None, None, *ints(kw, *ALL), 1.0, 1, None)
+        return L.hla2_window_backward(ODD, P, P, P, P, P, P, P, P, None, *ints(kw, *ALL), 1.0, 1, None, 0, None)
+
+    small = dict(d=16, dv=16, window=8, sinks=0)
+    for call in ("forward", "cache", "backward"):
+        for good in (dict(B=1 << 9, H=8, Hkv=8, n=1 << 16), dict(B=1 << 9, H=32, Hkv=32, n=1 << 15),
+                     dict(B=1, H=(1 << 18) - 1, Hkv=(1 << 18) - 1, n=1 << 12)):
+            assert good["B"] * good["H"] * good["n"] >= 1 << 28
+            assert code(call, **small, **good) == INV
+        assert code(call, **small, B=1, H=1 << 18, Hkv=1 << 18, n=1 << 12) == UNS
+    assert H.hla2_window_backward_workspace_bytes(*ints(dict(small, B=1 << 9, H=8, Hkv=8, n=1 << 16), *ALL), 1) == 4 << 28
