@@ -386,9 +386,9 @@ def test_log_gates_that_hold(size, constant, use_s0, dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_decay_of_a_state_by_a_log_gate(dtype):
-    """n tokens of one gate and no input: s = exp(n g) s0.  A token's factor is off by at most 4 u of 1 - a (the series' rest, three multiply-adds and
-    one product) or 4 u of a, and its product by u / 2; so 4 u n |g| + u n in all, and 12 u for the tiles' maps
-    of each 256 tokens."""
+    """n tokens of one gate and no input: s = exp(n g) s0.  A token's factor is off by at most 4 u of 1 - a (the
+    series' rest, three multiply-adds and one product) or 4 u of a, and its product by u; so 4 u n |g| + u n in
+    all, and 12 u for the tiles' maps of each 256 tokens."""
     n, g = 5000, torch.tensor([-2.0 ** -k for k in range(2, 24)])
     c = dict(x=torch.zeros(1, 1, n, 22), g=g.expand(1, 1, n, 22).contiguous(), s0=torch.ones(1, 1, 22),
              dout=torch.zeros(1, 1, n, 22), ds_last=torch.ones(1, 1, 22))
