@@ -250,11 +250,12 @@ template <int CS> __device__ __forceinline__ Word *words_of(const GatedArgs &p, 
 // Forward.  A thread forms the map of its R tokens, (A, H) with s -> A s + H, A held; the thread rows' maps are
 // folded in LDS in quarters by all threads, the quarters by the first CS, which also carry the state in
 // from the tile before; then every thread walks its tokens again from the state it starts with.
-// Bound by HBM: x and g read once, out written once.  8 x 16 heads x 8192 tokens, d = 128, bf16, log gate:
-// 158 us, 5.1 TB/s, the rate of a large copy (two passes over x and g would move 5/3 of that); 65536 tokens
-// x 2048 channels, sigmoid: 168 us.  256 tokens to a tile: a thread's 8 rows of 16 bytes keep 64 KB of
+// Bound by HBM and, in bf16, as nearly by the vector units: x and g read once, out written once.  8 x 16 heads x
+// 8192 tokens, d = 128, bf16, log gate: 163 us, 4.9 TB/s, where a large copy reaches 5.1 (two passes over x and
+// g would move 5/3 of that) and vector instructions issue in every cycle; 65536 tokens x 2048 channels,
+// sigmoid: 178 us, in 86% of them.  256 tokens to a tile: a thread's 8 rows of 16 bytes keep 64 KB of
 // loads in flight to a workgroup, and a tile's words are 1% of its data.  Three workgroups to a compute
-// unit: at four (128 registers) the look-back's words spill.
+// unit or, where 128 registers are enough, four.
 template <typename T, int GATE, bool VEC>
 __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
   using S = Shape<T, VEC>;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(256, 3) gated_forward_kernel(GatedArgs p) {
 }
 
 // Backward.  Bound by HBM: x, g and dout read once, dx and dg written once (65536 tokens x 2048 channels,
-// bf16, sigmoid: 275 us, 4.9 TB/s; with the gate formed anew at each use 325).  The tile's states are
+// bf16, sigmoid: 280 us, 4.8 TB/s; with the gate formed anew at each use 18% more).  The tile's states are
 // recomputed from its mark, so the only carry is the adjoint's, u = a r, which runs from the last tile to
 // the first: turn 0 is the sequence's last tile.
 template <typename T, int GATE, bool VEC>

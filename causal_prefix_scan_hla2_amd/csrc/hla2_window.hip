@@ -9,14 +9,17 @@
 //
 // A workgroup holds 128 rows of a head (64 where the grid would be small), a wave 32 of them, so that a
 // fragment of K or V read from LDS feeds two products; the next tile of 64 keys is on its way from
-// memory meanwhile.  Vector and matrix units share a SIMD's issue slots: at d = 64, dv = 128 a wave's
-// tile is 48 matrix and 200 vector instructions (the exponentials twice), at d = dv = 128 64 and 200.
-// Measured: 8 x 16 heads x 8192 tokens, d = 64, dv = 128, window 1024: 0.60 ms, 0.65 PFLOP/s; 16 heads x
-// 65536 tokens, d = dv = 128, window 2048: 1.23 ms, 0.89 PFLOP/s, where a library product of 8192 x 8192
-// matrices reaches 1.2.  Slower: 16 rows to a wave and four waves to a SIMD (764 against 706 us at the first
-// shape), 64 rows to a wave (1092), 256 rows to a workgroup (773), the next tile's scores formed during
-// this one's softmax (730), two tiles on their way (711).  Without barriers it would be 6% faster,
-// without the tiles' loads and stores 25%.
+// memory meanwhile.  At d = 64, dv = 128 a wave's tile is 48 matrix and 200 vector instructions (the
+// exponentials twice), at d = dv = 128 64 and 200.
+// Measured: 8 x 16 heads x 8192 tokens, d = 64, dv = 128, window 1024: 0.59 ms, 0.66 PFLOP/s; 16 heads x
+// 65536 tokens, d = dv = 128, window 2048: 1.21 ms, 0.90 PFLOP/s, where a library product of 8192 x 8192
+// matrices reaches 1.2.  No unit is full: matrix units 32% and 43% of the cycles, vector issue 53% and 51%, LDS
+// 25% and 33%.  What is left are waits that the two waves of a SIMD do not cover for each other: without the
+// tiles' loads and stores, through registers into LDS, it would be 25% faster, without barriers 6%.
+// Sizes of d and dv between the instantiations are padded to the next, products and all.
+// Slower: 16 rows to a wave and four waves to a SIMD (764 against 706 us at the first shape), 64 rows to a wave
+// (1092), 256 rows to a workgroup (773), the next tile's scores formed during this one's softmax (730), two
+// tiles on their way (711).
 #include "hla2.h"
 #include "hla2_window.h"
 

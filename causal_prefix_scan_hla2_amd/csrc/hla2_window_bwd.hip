@@ -9,11 +9,11 @@
 // runs, each head's run summed by a workgroup of its own, in the same launch, into the workspace, where the
 // walk of those keys leaves its sums too; a launch of one thread to four sums adds them up, in order.
 //
-// Measured at 16 heads (4 key heads) x 65536 tokens, d = dv = 128, window 2048, 16 sinks: dq 1.91 ms (1.2
-// PFLOP/s with ds in two operands), dk and dv with the far queries 2.65 ms (0.9), their sum 0.02 ms.  dq is bound
-// by the issue of vector and matrix instructions, dk and dv by LDS: a wave holds 16 keys at d = 128
-// (registers), so each fragment feeds one product.  Slower there: 32 keys to a wave with one wave to a
-// SIMD (3.3 against 2.5 ms), or with v in LDS and one buffer (4.7, spills); below, 32 keys fit.
+// Measured at 16 heads (4 key heads) x 65536 tokens, d = dv = 128, window 2048, 16 sinks: dq 1.90 ms (1.2
+// PFLOP/s with ds in two operands), dk and dv with the far queries 2.68 ms (0.9), their sum 0.02 ms.  dq has the
+// matrix units busy in 57% of the cycles and vector issue in 54%; dk and dv 38% and 36%, with LDS at 53%: a wave
+// holds 16 keys at d = 128 (registers), so each fragment feeds one product.  Slower there: 32 keys to a wave with
+// one wave to a SIMD (3.3 against 2.5 ms), or with v in LDS and one buffer (4.7, spills); below, 32 keys fit.
 #include "hla2.h"
 #include "hla2_window.h"
 

@@ -399,9 +399,9 @@ int hla2_gated_scan_step(float *state, const void *x, const void *g, void *out, 
  *   window >= 1 (window >= n: causal attention), 0 <= sinks <= HLA2_WINDOW_MAX_SINKS,
  *   scale > 0 and finite (below 2^126)
  * Outputs overlap neither the inputs nor each other, here and in the calls below.
- * Supported: d, dv multiples of 16 up to 128 (fp32: up to 64); B * H * ceil(n / 64)
- * below 2^24 - 8; the other limits and errors as for hla2_forward; tensors 16-byte
- * aligned.  For finite inputs a row
+ * Supported: d, dv multiples of 16 up to 128 (fp32: up to 64), computed as the next of
+ * 64 and 128; B * H * ceil(n / 64) below 2^24 - 8; the other limits and errors as for
+ * hla2_forward; tensors 16-byte aligned.  For finite inputs a row
  * does not depend on tokens it does not see; a NaN or Inf in a token before the
  * sequence's end can reach rows that do not see it (0 * Inf = NaN).
  */
@@ -416,6 +416,12 @@ int hla2_window_forward(const void *q, const void *k, const void *v, void *out, 
  *   dq_t = scale sum_j ds_tj k_j,  dk_j = scale sum_t ds_tj q_t,  dv_j = sum_t p_tj dout_t,
  * dk and dv summed over the query heads that share a key head.  No gradient is
  * formed through lse.  Results do not depend on the order of execution.
+ * Sums are fp32.  For bf16 the operands of the products are rounded to bf16: the
+ * weights p for dv and ds for dk once, but in what is left over as well on the tiles
+ * at a window's ends (for dv where a wave holds 16 keys: windows below 128, few rows,
+ * d or dv above 64); ds for dq always in both parts.  D comes from the rounded out,
+ * or for bf16 from the weights where a block of queries sees at most five tiles of 64
+ * keys.
  *   q, k, v, out, lse, lens: those of the forward call; dout [B, H, n, dv]
  *   dq, dk, dv_out: as q, k, v (written); rows behind a sequence's end are left
  *   workspace: at least hla2_window_backward_workspace_bytes(...) bytes, 256-byte
