@@ -12,15 +12,18 @@ namespace {
 
 static_assert(GATED_TILE == HLA2_GATED_SCAN_TILE, "marks are a tile apart");
 
-// A gate in one register, "held": the factor a, 0 <= a <= 1, as -a where it is small and as z = 1 - a, which is
-// formed by itself and not by subtraction, where it is not.  A gate that holds its state for 1/z tokens is
-// off by z's relative error then, whatever z; 1 - a from a rounded a is off by 2^-25 / z, and every token adds that
-// (9000 tokens of a constant sigmoid gate near logit 12: 4e-3, near 18: 0.5).  The factor not held is 1 minus the
-// one that is, good to half a step.  The sign is the whole sign bit: -0 is a = 0, +0 is z = 0.
+// A gate in one register, "held": the factor a, 0 <= a <= 1, as -a where it is small and as z = 1 - a, which
+// is formed by itself and not by subtraction, where it is not.  A gate that holds its state for 1/z tokens
+// is off by z's relative error then, whatever z; 1 - a from a rounded a is off by 2^-25 / z, and every token
+// adds that (states after 9000 tokens of a constant sigmoid gate near logit 12: 4e-3 off, near 18: 0.7).  The
+// factor not held is 1 minus the one that is, good to half a step.  The sign is the whole sign bit: -0 is
+// a = 0, +0 is z = 0.
 __device__ __forceinline__ bool held_a_itself(float h) { return __builtin_bit_cast(int, h) < 0; }
 __device__ __forceinline__ float held_z(float h) { return held_a_itself(h) ? 1.f + h : h; }
 // a s + y
-__device__ __forceinline__ float scale_add(float h, float s, float y) { return fmaf(-h, s, y) + (held_a_itself(h) ? 0.f : s); }
+__device__ __forceinline__ float scale_add(float h, float s, float y) {
+  return fmaf(-h, s, y) + (held_a_itself(h) ? 0.f : s);
+}
 // a u
 __device__ __forceinline__ float scale(float h, float u) { return fmaf(-h, u, held_a_itself(h) ? 0.f : u); }
 
@@ -37,7 +40,9 @@ template <bool FAST> __device__ __forceinline__ float hold_exp(float m) {
   return m > -0.0625f ? fabsf(z) : -a;  // of a NaN, a
 }
 // What the gate is formed from: log gates above 0 count as 0 (a NaN stays).
-template <int GATE> __device__ __forceinline__ float gate_arg(float g) { return GATE == HLA2_GATE_LOG && g > 0.f ? 0.f : g; }
+template <int GATE> __device__ __forceinline__ float gate_arg(float g) {
+  return GATE == HLA2_GATE_LOG && g > 0.f ? 0.f : g;
+}
 template <typename T, int GATE> __device__ __forceinline__ float hold(float arg) {
   constexpr bool FAST = sizeof(T) == 2;
   if constexpr (GATE == HLA2_GATE_LOG) {
@@ -139,9 +144,9 @@ template <int R, int V> __device__ __forceinline__ void fresh(float (&x)[R][V]) 
 
 // ---------------------------------------------------------------------------
 // Carries between the tiles of one sequence.  A tile is the map s -> A s + H of the state it starts
-// from, A held like a gate.  Its workgroup publishes (A, H), then looks back for the newest tile whose outgoing state is
-// known and folds the maps in between onto it, oldest first: the same multiply-adds in the same order
-// as the tiles in between make themselves, so the result does not depend on what was found.
+// from, A held like a gate.  Its workgroup publishes (A, H), then looks back for the newest tile whose
+// outgoing state is known and folds the maps in between onto it, oldest first: the same multiply-adds in
+// the same order as the tiles in between make themselves, so the result does not depend on what was found.
 // What is published is one 64-bit word, written and read whole, so no ordering between words is needed:
 // a state beside a mark that it is there, or a map as H beside A's inverted bits, which are not zero.
 // The words are cleared by a launch before.
